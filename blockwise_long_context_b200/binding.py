@@ -276,6 +276,17 @@ def _launch(name: str, dev: int, stream, *args) -> None:
         raise LvxError(status, name)
 
 
+def _scratch(nbytes: int, dev: int, stream) -> torch.Tensor:
+    """A workspace for launches on `stream` (None: the current one), from the memory of that stream: what is
+    given the same memory once the workspace is dropped comes after the launches."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
 def _few(*sizes) -> None:
     """Sizes that the C entry points take as int."""
     if max(sizes) > 0x7fffffff:
@@ -407,8 +418,7 @@ def lvx_head_norm_rope_bwd(q, k, w_q, w_k, dq_out, dk_out, dq, dk, dw_q, dw_k, p
     wq_ = None if dw_q is None else _dense(dw_q, (d,), torch.float32, dev, "dw_q")
     wk_ = None if dw_k is None else _dense(dw_k, (d,), torch.float32, dev, "dw_k")
     if workspace is None:
-        workspace = torch.empty(lvx_head_norm_rope_bwd_workspace(d), dtype=torch.uint8,
-                                device=(q if q is not None else k).device)
+        workspace = _scratch(lvx_head_norm_rope_bwd_workspace(d), dev, stream)
     elif workspace.get_device() != dev:
         raise ValueError(f"workspace is on {workspace.device}, not on cuda:{dev}")
     _launch("lvx_head_norm_rope_bwd", dev, stream, q_, k_, _weight(w_q, ref, "w_q"),
@@ -461,7 +471,7 @@ def lvx_attn_prefix(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_len, out, 
     q_, out_ = _dense(q, shape, dtype, _device(q), "q"), _dense(out, shape, dtype, dev, "out")
     lse_ = _dense(lse, (B, H, S_Q), torch.float32, dev, "lse")
     if workspace is None:
-        workspace = prefix_workspace(q, H_kv, S_P, S_cap)
+        workspace = prefix_workspace(q, H_kv, S_P, S_cap, stream)
     elif workspace.get_device() != dev:
         raise ValueError(f"workspace is on {workspace.device}, not on cuda:{dev}")
     _launch("lvx_attn_prefix", dev, stream, q_, kp_, vp_, ks_, vs_, n_, out_, lse_, B, H, H_kv, S_Q,
@@ -598,15 +608,15 @@ def head_norm_rope_backward(q, k, w_q, w_k, dq_out, dk_out, pos=None, inv_freq=N
     return dq, dk, dw_q, dw_k
 
 
-def prefix_workspace(q, H_kv: int, S_P: int, S_cap: int) -> torch.Tensor:
-    """The workspace of lvx_attn_prefix for queries like q."""
+def prefix_workspace(q, H_kv: int, S_P: int, S_cap: int, stream=None) -> torch.Tensor:
+    """The workspace of lvx_attn_prefix for queries like q, for calls on `stream` (None: the current one)."""
     if not q.is_cuda:
         raise ValueError("tensors must be contiguous CUDA tensors")
     B, S_Q, H, d = q.shape
     nbytes = lvx_attn_prefix_workspace(B, H, H_kv, S_Q, S_P, S_cap, d, _dt(q))
     if nbytes == 0:
         raise LvxError(2, "prefix_workspace: invalid or unsupported shape")
-    return torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    return _scratch(nbytes, q.get_device(), stream)
 
 
 def attention_prefix(q, k_prefix, v_prefix, k_suffix=None, v_suffix=None, suffix_len=None,
