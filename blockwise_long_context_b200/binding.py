@@ -67,6 +67,7 @@ _SIGS = {
     "lvx_attn_prefix": ([_vp] * 8 + [_c_int] * 7 + [_c_int, _c_float, _vp, _c_size, _vp], _c_int),
     "lvx_last_device_error": ([_vp], _c_int),
     "lvx_selftest_wait_timeout": ([_vp], _c_int),
+    "lvx_selftest_prefix_plan": ([_c_int] * 7 + [_c_int, _vp], _c_int),
 }
 
 
@@ -484,6 +485,16 @@ def lvx_last_device_error(stream=None) -> None:
 
 def lvx_selftest_wait_timeout(stream=None) -> None:
     _check(lib().lvx_selftest_wait_timeout(_stream(stream)), "lvx_selftest_wait_timeout")
+
+
+def lvx_selftest_prefix_plan(B, H, H_kv, S_Q, S_P, S_cap, d, dtype: int) -> dict:
+    """How lvx_attn_prefix takes a problem of these sizes: the kernels ("rows", "tc" or "fp32") of the
+    prefix's and the suffixes' parts, the parts and their keys, and whether it takes requests whole."""
+    plan = (_c_int * 7)()
+    _check(lib().lvx_selftest_prefix_plan(B, H, H_kv, S_Q, S_P, S_cap, d, dtype, plan), "lvx_selftest_prefix_plan")
+    kernels = ("rows", "tc", "fp32")
+    return {"prefix": kernels[plan[0]], "suffix": kernels[plan[1]], "n_pre": plan[2], "pre_len": plan[3],
+            "n_suf": plan[4], "suf_len": plan[5], "whole": bool(plan[6])}
 
 
 # ------------------------------------------------------------------ conveniences

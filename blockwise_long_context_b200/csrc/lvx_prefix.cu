@@ -402,4 +402,18 @@ lvx_status lvx_attn_prefix(const void* q, const void* k_prefix, const void* v_pr
   return e == cudaSuccess ? LVX_OK : LVX_ERR_CUDA;
 }
 
+lvx_status lvx_selftest_prefix_plan(int B, int H, int H_kv, int S_Q, int S_P, int S_cap, int d, lvx_dtype dt,
+                                    int plan[7]) {
+  const lvx_status st = check_prefix(B, H, H_kv, S_Q, S_P, S_cap, d, dt);
+  if (st != LVX_OK) return st;
+  if (!plan) return LVX_ERR_INVALID_ARG;
+  const PrefixPlan x = plan_prefix(B, H, H_kv, S_Q, S_P, S_cap, d, dt, 0.f);
+  // whole requests: the few-row kernel in bf16, whatever the parts would have taken
+  const bool rows = x.whole && x.pre != kPrefixFp32;
+  const int values[7] = {rows ? kPrefixRows : x.pre, rows ? kPrefixRows : x.suf, x.p.n_pre, x.p.pre_len,
+                         x.p.n_suf, x.p.suf_len, x.whole};
+  std::copy(values, values + 7, plan);
+  return LVX_OK;
+}
+
 }  // extern "C"

@@ -426,6 +426,17 @@ lvx_status lvx_last_device_error(lvx_stream stream);
  */
 lvx_status lvx_selftest_wait_timeout(lvx_stream stream);
 
+/*
+ * Diagnostic: how lvx_attn_prefix takes a problem of these sizes (nothing is
+ * launched; its checks and codes).  plan[0], plan[1]: the kernel of the prefix's
+ * parts and of the suffixes' parts, 0 the few-row kernel, 1 the tcgen05 kernel,
+ * 2 the fp32 kernel.  plan[2], plan[3]: parts of the prefix and keys of each;
+ * plan[4], plan[5]: parts of a suffix and keys of each.  plan[6] = 1: every request
+ * whole in one block per 16 (few-row) or up to 32 (fp32) rows, without parts.
+ */
+lvx_status lvx_selftest_prefix_plan(int B, int H, int H_kv, int S_Q, int S_P, int S_cap, int d,
+                                    lvx_dtype dt, int plan[7]);
+
 #ifdef __cplusplus
 }
 #endif
