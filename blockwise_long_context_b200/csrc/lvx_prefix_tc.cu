@@ -342,6 +342,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap map_qp, const __grid_consta
           if (done) l_sum += sum;
         }
         if (!done) {
+          tmem_wait_st();   // P is stored again below: two stores to one place keep no order of their own
           if (key0 + BK > lim_min) {
 #pragma unroll
             for (int i = 0; i < BK; ++i)
