@@ -45,6 +45,7 @@ static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= 65536 / kThreads * kThr
               "register split exceeds the launch allocation");
 constexpr uint32_t CHUNK = 128 * 128;   // one TMA box: 128 rows x 64 bf16 (128 B), swizzled
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
+constexpr float kNoMaximum = -3e38f;
 constexpr float kRescaleFactor = 256.0f;    // 2^kRescaleThreshold
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -388,6 +389,10 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           m_ref = m_tile;
           l_sum *= alpha;
         }
+        // A row whose scores are all NaN or -inf so far: the lowest maximum there is, which any
+        // number moves, so that the warp's rows leave the first tile together (its votes and
+        // tcgen05.ld/st are for all lanes; masked tiles are a block's last ones).
+        if (!need_mask && m_ref == -INFINITY) m_ref = kNoMaximum;
         if (j > 0 && __any_sync(0xffffffffu, resc)) {
           // O_t is quiescent here: P_t V of tile j-1 finished before S_t of tile j was issued
 #pragma unroll 1
@@ -457,7 +462,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     if (T > 0 && ok) ok = ptx::mbar_wait(&o_done[t], (T - 1) & 1, a.err, kErrTimeoutEpilogue, abort_flag);
     ok = __all_sync(0xffffffffu, ok);
     ptx::tc_fence_after();
-    const bool seen = T > 0 && l_sum > 0.f;
+    const bool seen = T > 0 && l_sum > 0.f && m_ref > kNoMaximum;
     const float inv_l = seen ? 1.f / l_sum : 0.f;
     const float Lrow = seen ? (m_ref + __log2f(l_sum)) * kLn2 : -INFINITY;
     const bool write = ok && row < p.S_Q;
