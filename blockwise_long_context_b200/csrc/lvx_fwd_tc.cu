@@ -364,6 +364,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         wait_upper();
       }
       if (!done) {
+        ptx::tmem_wait_st();   // P is stored again below: two stores to one place keep no order of their own
         if (need_mask) {
           const int lim = p.causal ? min(kb1, row + 1) : kb1;   // keys [key0, lim) visible
 #pragma unroll
