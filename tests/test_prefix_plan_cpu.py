@@ -50,3 +50,21 @@ def test_refusals(shape, code):
     with pytest.raises(lvx.LvxError) as e:
         lvx.lvx_selftest_prefix_plan(*shape, lvx.LVX_BF16)
     assert e.value.status == code
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("shape", [
+    (1, 32, 8, 4096, 65536, 65536, 128), (8, 32, 8, 2048, 1000, 32768, 128), (1, 32, 8, 1024, 1000, 65536, 128),
+    (128, 32, 8, 1, 1, 65536, 128), (16, 16, 16, 512, 0, 100000, 64), (64, 28, 4, 4, 100, 20000, 80)])
+def test_long_caches_take_a_bounded_workspace(shape, dt):
+    """The parts of many rows over long caches stay below what the caches themselves take."""
+    B, H, H_kv, S_Q, S_P, S_cap, d = shape
+    caches = 2 * B * S_cap * H_kv * d * (4 if dt == lvx.LVX_FP32 else 2)
+    assert lvx.lvx_attn_prefix_workspace(*shape, dt) <= caches
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_short_parts_where_there_are_few_blocks(dt):
+    """One request over a long cache: its parts are what fills the machine."""
+    p = lvx.lvx_selftest_prefix_plan(1, 32, 8, 1, 0, 65536, 128, dt)
+    assert p["suf_len"] <= 512 and p["n_suf"] * 8 >= 148, p
