@@ -16,7 +16,8 @@
 // off by |pos| * 2^-54 turns at most for frequencies up to 1 (F comes from a double product).
 // The top 32 bits go to a float.  16-bit outputs take the special-function unit's
 // sine and cosine (absolute error below 2^-20 on [-pi, pi], against the 2^-9 of
-// the output's rounding); 32-bit outputs take sincospif.
+// the output's rounding); 32-bit outputs take the Taylor series of the remainder to the
+// nearest quarter turn (off by 1.6 x 2^-24 at most).
 //
 // All three are bound by HBM: 2 (forward) or 3 (backward) streams of
 // (H + H_kv) d elements a token, a few operations an element.  A group of LP lanes
@@ -262,14 +263,27 @@ __device__ __forceinline__ uint64_t turn_fraction(float inv_freq) {
 // (cos, sin) of the angle F turns times pos.
 template <typename T>
 __device__ __forceinline__ float2 turn_of(uint64_t F, int pos, bool back) {
-  const int phase = (int)(uint32_t)((F * (uint64_t)(int64_t)pos) >> 32);
-  const float t = (float)phase * 2.3283064365386963e-10f;   // turns in [-1/2, 1/2]
+  const uint32_t phase = (uint32_t)((F * (uint64_t)(int64_t)pos) >> 32);
   float2 cs;
   if (sizeof(T) == 2) {
+    const float t = (float)(int)phase * 2.3283064365386963e-10f;   // turns in [-1/2, 1/2]
     cs.x = __cosf(t * 6.283185307179586f);
     cs.y = __sinf(t * 6.283185307179586f);
   } else {
-    sincospif(2.f * t, &cs.y, &cs.x);
+    // the remainder x to the nearest quarter turn (two bits more than a float of the whole turn
+    // keeps), and the Taylor series of sin 2 pi x and cos 2 pi x, which end below 2^-29 at x = 1/8
+    constexpr double w = 6.283185307179586477, w2 = w * w, w4 = w2 * w2;
+    const uint32_t quarter = (phase + (1u << 29)) >> 30;
+    const float x = (float)(int)(phase - (quarter << 30)) * 2.3283064365386963e-10f, x2 = x * x;
+    float p = fmaf((float)(w4 * w4 * w / 362880), x2, (float)(-w4 * w2 * w / 5040));
+    p = fmaf(fmaf(p, x2, (float)(w4 * w / 120)), x2, (float)(-w2 * w / 6));
+    const float sn = fmaf(x, (float)w, x * fmaf(x2, p, (float)(w - (float)w)));
+    float q = fmaf((float)(-w4 * w4 * w2 / 3628800), x2, (float)(w4 * w4 / 40320));
+    q = fmaf(fmaf(q, x2, (float)(-w4 * w2 / 720)), x2, (float)(w4 / 24));
+    const float c = fmaf(x2, fmaf(x2, q, (float)(-w2 / 2)), 1.f);
+    const float u = quarter & 1 ? sn : c, v = quarter & 1 ? c : sn;
+    cs.x = (quarter + 1) & 2 ? -u : u;
+    cs.y = quarter & 2 ? -v : v;
   }
   if (back) cs.y = -cs.y;
   return cs;
