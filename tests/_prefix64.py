@@ -40,14 +40,14 @@ def attention(q, kp, vp, ks, vs, lens, scale=None):
     return out, lse, mag
 
 
-def check(out, lse, args, scale=None, what="", rows=None):
-    """The outputs against 64 bits; rows [B, S_Q, H]: those that count."""
+def check(out, lse, args, scale=None, what="", rows=None, kmax=None):
+    """The outputs against 64 bits; rows [B, S_Q, H]: those that count; kmax: norm of the longest key that does."""
     q, kp, vp, ks, vs, n = args
     ref, ref_l, mag = attention(*args, scale=scale)
     d = q.shape[-1]
     sc = d ** -0.5 if scale is None else scale
     longest = lambda x: float(x.float().nan_to_num(0, 0, 0).norm(dim=-1).max())  # noqa: E731
-    kmax = max(longest(x) for x in (kp, ks) if x is not None and x.numel())
+    kmax = kmax or max(longest(x) for x in (kp, ks) if x is not None and x.numel())
     keys = sum(x.shape[-3] for x in (kp, ks) if x is not None)
     e = (d + 2) * V * sc * q.double().norm(dim=-1) * kmax          # [B, S_Q, H]
     r = 2.0 ** -8 if q.dtype == torch.bfloat16 else 0.0

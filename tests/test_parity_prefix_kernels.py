@@ -60,3 +60,100 @@ def test_rising_scores(shape, prefix, suffix):
     for _ in range(5):
         assert all(torch.equal(x, y) for x, y in zip(lvx.attention_prefix(*args), first))
     lvx.lvx_last_device_error()
+
+
+def _garbage(args):
+    """NaN and infinities behind every request's last key."""
+    n = args[5].long().clamp(0, args[3].shape[1])
+    behind = torch.arange(args[3].shape[1], device="cuda") >= n[:, None]
+    args[3][behind] = float("nan")
+    args[4][behind] = float("nan")
+    args[4][:, ::2][behind[:, ::2]] = float("inf")
+
+
+LENGTHS = [0, 1, 2, 63, 64, 65, 127, 129, 255, 256, 257, 511, 512, 513, 600, 1023, 1024, 1025, 2047, 2049, 9999, -3]
+
+
+@pytest.mark.parametrize("shape,prefix,suffix", [
+    # the tensor-core kernel's head widths, and heads a group that do and do not divide its 128 rows
+    ((40, 8, 4, 50, 0, 65, 8), None, "tc"),
+    ((8, 10, 2, 130, 65, 300, 8), "tc", "tc"),
+    ((8, 66, 2, 9, 300, 513, 40), "tc", "tc"),         # 33 heads: 3 tokens a tile
+    ((1, 65, 1, 50, 1000, 1100, 40), "tc", "tc"),      # one token a tile
+    ((16, 7, 1, 50, 300, 513, 40), "tc", "tc"),
+    ((16, 16, 4, 17, 300, 513, 64), "tc", "tc"),
+    ((5, 4, 4, 130, 3000, 1100, 64), "tc", "tc"),      # two row tiles of a request
+    ((16, 260, 4, 4, 0, 65, 64), None, "tc"),
+    ((40, 4, 4, 130, 300, 65, 72), "tc", "tc"),
+    ((24, 12, 4, 100, 0, 300, 72), None, "tc"),
+    ((24, 4, 2, 64, 0, 1100, 80), None, "tc"),         # five parts
+    ((40, 20, 4, 17, 300, 65, 80), "tc", "tc"),
+    ((24, 12, 4, 17, 300, 1100, 96), "tc", "tc"),
+    ((2, 256, 2, 17, 300, 130, 96), "tc", "tc"),       # 128 heads a group
+    ((3, 12, 4, 130, 300, 513, 128), "tc", "tc"),
+    ((2, 28, 4, 100, 65, 700, 128), "tc", "tc"),
+    ((1, 100, 1, 50, 300, 513, 128), "tc", "tc"),
+    # the few-row kernel beside it, and alone in parts
+    ((6, 8, 2, 40, 2000, 800, 128), "tc", "rows"),
+    ((3, 4, 1, 2, 5000, 700, 72), "rows", "rows"),
+    # parts of more than 512 keys
+    ((90, 16, 4, 1, 200, 6000, 64), "rows", "rows"),
+    ((40, 32, 4, 16, 100, 9000, 128), "tc", "tc"),
+])
+def test_ragged_lengths_with_garbage_behind_them(shape, prefix, suffix):
+    plan = _plan(*shape)
+    assert prefix in (None, plan["prefix"]) and suffix in (None, plan["suffix"]) and not plan["whole"], plan
+    cap = shape[5]
+    for turn in (0, 7, 14):
+        lens = [n for n in LENGTHS[turn:] + LENGTHS[:turn] if n <= cap or n == 9999] + [cap - 1, cap]
+        args = _make(*shape, seed=turn, lens=lens)
+        _garbage(args)
+        first = lvx.attention_prefix(*args)
+        check(*first, args, what=f"{plan} {lens}")
+        for _ in range(3):
+            assert all(torch.equal(x, y) for x, y in zip(lvx.attention_prefix(*args), first))
+    lvx.lvx_last_device_error()
+
+
+@pytest.mark.parametrize("shape", [(4, 32, 8, 64, 300, 9000, 64), (100, 8, 2, 1, 50, 20000, 72)])
+def test_long_fp32_parts(shape):
+    plan = _plan(*shape, dt=torch.float32)
+    assert plan["suffix"] == "fp32" and plan["suf_len"] > 512, plan
+    args = _make(*shape, dt=torch.float32, lens=[shape[5], 0, 1, plan["suf_len"] - 1, plan["suf_len"], plan["suf_len"] + 1])
+    _garbage(args)
+    check(*lvx.attention_prefix(*args), args, what=str(plan))
+
+
+@pytest.mark.parametrize("shape,prefix,suffix", [((40, 20, 4, 17, 300, 65, 80), "tc", "tc"),
+                                                 ((16, 16, 4, 17, 300, 513, 64), "tc", "tc"),
+                                                 ((6, 8, 2, 40, 2000, 800, 128), "tc", "rows")])
+def test_nan_queries_stay_in_their_rows(shape, prefix, suffix):
+    plan = _plan(*shape)
+    assert (plan["prefix"], plan["suffix"]) == (prefix, suffix), plan
+    args = _make(*shape)
+    q = args[0]
+    clean = q.clone()
+    fine = torch.ones(q.shape[:3], dtype=torch.bool, device="cuda")
+    for b, t, h in ((0, 0, 0), (1, 5, 3), (shape[0] - 1, shape[3] - 1, shape[1] - 1)):
+        q[b, t, h, (b + t) % shape[6]] = float("nan")
+        fine[b, t, h] = False
+    out, lse = lvx.attention_prefix(*args)
+    assert torch.isnan(out[~fine]).all() and torch.isnan(lse.transpose(1, 2)[~fine]).all()
+    check(out, lse, [clean, *args[1:]], rows=fine, what=str(plan))
+
+
+@pytest.mark.parametrize("shape,prefix,suffix", [((40, 20, 4, 17, 300, 65, 80), "tc", "tc"),
+                                                 ((32, 32, 8, 1, 20000, 300, 128), "tc", "rows"),
+                                                 ((3, 4, 1, 2, 5000, 700, 72), "rows", "rows")])
+def test_first_keys_of_minus_infinity_for_some_rows(shape, prefix, suffix):
+    """The first 100 prefix keys' products overflow to -inf for every third row: weights of 0."""
+    plan = _plan(*shape)
+    assert (plan["prefix"], plan["suffix"]) == (prefix, suffix), plan
+    q, kp, vp, ks, vs, n = args = _make(*shape)
+    rows = torch.arange(q.shape[0] * q.shape[1] * q.shape[2], device="cuda").view(q.shape[:3]) % 3 == 0
+    q[..., 0] = 0
+    longest = max(float(x.float().norm(dim=-1).max()) for x in (kp, ks))
+    q[..., 0][rows] = 3
+    kp[..., 0] = ks[..., 0] = 0
+    kp[:100, :, 0] = -3e38
+    check(*lvx.attention_prefix(*args), args, what=str(plan), kmax=longest)
