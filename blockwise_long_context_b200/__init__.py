@@ -3,8 +3,9 @@
 The compute path is ``liblvx.so`` (C ABI, declared in ``include/lvx.h``):
 hand-written sm_100a kernels for the block partials, their merge, the
 backward pass, the K/V recomputation, positions and norms of queries and keys,
-and decoding over a shared prefix.  This package is a thin ctypes
-binding with the same entry-point names; it only marshals arguments (shapes,
+and decoding over a shared prefix.  This package is a thin
+binding with the same entry-point names (ctypes, and for the allocating calls of a
+decoding step the extension ``_calls.so``); it only marshals arguments (shapes,
 pointers, the current CUDA stream) and raises on error.  PyTorch supplies
 device memory and streams.  There is no fallback: if the library is missing
 every call raises.

@@ -1,9 +1,11 @@
-"""ctypes binding of liblvx.so (argument marshalling only).
+"""Binding of liblvx.so (argument marshalling only), by ctypes.
 
 Each ``lvx_*`` function here has the C entry point's name and meaning (see
 ``include/lvx.h``).  Sizes are read from tensor shapes, pointers from
 ``data_ptr()``, the stream from ``torch.cuda.current_stream()`` unless one is
-given.  Every step of the computation runs in the library's kernels.
+given.  Every step of the computation runs in the library's kernels.  Four allocating calls
+(rope_axes, head_norm_rope, head_norm_rope_backward, attention_prefix) go through the
+extension ``_calls.so``, which takes their arguments in less time.
 """
 
 from __future__ import annotations
@@ -437,7 +439,8 @@ def lvx_attn_prefix(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_len, out, 
                     scale: float = 0.0, workspace: Optional[torch.Tensor] = None,
                     stream=None) -> None:
     """q [B,S_Q,H,d], a shared prefix k/v [S_P,H_kv,d], suffix caches k/v [B,S_cap,H_kv,d] of which
-    suffix_len [B] int32 keys are valid (either pair may be None) -> out like q, lse [B,H,S_Q] fp32."""
+    suffix_len [B] int32 keys are valid (either pair may be None) -> out like q, lse [B,H,S_Q] fp32.
+    A workspace that the call takes itself belongs to `stream`."""
     shape = q.shape
     if len(shape) != 4:
         raise ValueError("q must be [B, S_Q, H, d]")

@@ -4,9 +4,10 @@
 // n_b valid suffix keys, the visible keys are all S_P prefix keys and the suffix keys
 // j <= n_b - S_Q + t (the S_Q tokens are the request's last):
 //   O = sum softmax(s q.k) v,   LSE = ln sum exp(s q.k)   over them.
-// The keys are cut into parts, each part's (O_i, L_i) is computed by one block for
-// all rows that read the part's keys, and the parts are merged by the framework's
-// rescaling: L = M + ln sum exp(L_i - M), O = sum exp(L_i - L) O_i.
+// The keys are cut into parts, each part's (O_i, L_i) is computed by one block for a
+// tile of the rows that read the part's keys (128, 16 or up to 32, by the kernel), and
+// the parts are merged by the framework's rescaling: L = M + ln sum exp(L_i - M),
+// O = sum exp(L_i - L) O_i.  Requests of few keys are computed whole, without parts.
 #include <math.h>
 #include <stdint.h>
 

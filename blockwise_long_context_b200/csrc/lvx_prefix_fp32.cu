@@ -15,8 +15,10 @@
 // The slices' (m, l, O) are merged in shared memory.  Where a request has few keys, prefix
 // and suffix together, a block takes them all and writes the output itself (`whole`).
 //
-// Bound: 4 rows are bound by HBM (2 operations a byte; the machine does 11): 16384 keys of 8
-// heads of 128, 134 MB, 37 us.  32 rows are bound by fp32 multiply-adds, of which the
+// Bound: 4 rows do 2 operations a byte (the machine 11) and wait for their copies: with one
+// buffer each for K and V and block-wide barriers around them, one tile of a block is on its way
+// on average.  16384 keys of 8 heads of 128, 134 MB, 37 us, 55% of the copy rate.  32 rows are
+// bound by fp32 multiply-adds, of which the
 // two or three warps a scheduler holds keep 40% busy (128 rows x 32 heads over 2048 keys
 // 154 us, 28 TFLOP/s).  Slabs of 16 rows and packed multiply-adds were no faster.
 #include <type_traits>

@@ -11,8 +11,8 @@
 // first product in the layout in which the second takes them, and no warp waits for
 // another until the end.
 //
-// A block computes one part for one key/value head and 16 rows.  Its 4 warps take the part's
-// 32-key tiles in turn, each through a ring of its own (cp.async, 16 bytes a lane,
+// A block computes one part for one key/value head and 16 rows.  Its 4 warps (2 for parts of up
+// to 64 keys) take the part's 32-key tiles in turn, each through a ring of its own (cp.async, 16 bytes a lane,
 // rows of 2 DP bytes with their 16-byte words swapped by key mod 8 so that ldmatrix reads
 // without bank conflicts).  Keys past the part's end arrive as zeros, whatever the cache
 // holds, and are masked.  The warps' (m, l, O) are merged in shared memory.

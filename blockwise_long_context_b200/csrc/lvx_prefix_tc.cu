@@ -5,8 +5,8 @@
 // One CTA computes one part (O_i, L_i) for up to 128 query rows that read the same
 // keys: the G = H / H_kv query heads of a key/value head, times the tokens of all
 // requests (a part of the prefix) or of one request (a part of its suffix).  The
-// prefix is thus read once for the whole batch, whatever the batch, and a row tile
-// is full of queries where a tile per query head would hold S_Q rows.  Row i of a
+// prefix is thus read once for 128 rows of the batch (by further row tiles from L2),
+// and a row tile is full of queries where a tile per query head would hold S_Q rows.  Row i of a
 // tile is head i % G of the group, token i / G: the box {64, G, tokens} of a TMA
 // copy of q lands in that order.
 //
@@ -24,8 +24,9 @@
 //   S_j = Q K_j^T into one of two TMEM buffers, so that S_{j+1} runs during the
 //   softmax of S_j; P_j (bf16) is written over S_j; O += P_j V_j (A from TMEM).
 // The running maximum moves only when it grows by more than 2^8, as in the block
-// forward.  P is rounded to bf16 for the product (half a step, 2^-9 of each weight's
-// own size at most 2^-8); the row sum adds the unrounded fp32 weights.
+// forward.  P is rounded to bf16 for the product (half a step, at most 2^-8 of each
+// weight), the type in which V and the matrix unit take it; the row sum adds the
+// unrounded fp32 weights.
 //
 // Keys past a request's length.  The cache behind them may hold anything: their
 // scores are replaced by -inf, and their rows of V are zeroed in shared memory

@@ -345,7 +345,8 @@ lvx_status lvx_rope_axes(const void* q, const void* k, void* q_out, void* k_out,
  *   y = R(pos) (w o x / sqrt(mean(x^2) + eps))   over each head row x of d elements.
  *   w_q, w_k [d] (dtype dt), or NULL for ones.  n_freq == 0 leaves the rotation
  *   out (pos, inv_freq and axis_of are ignored).  eps >= 0.  Statistics are
- *   float32.  The rest as for lvx_rope_axes.
+ *   float32: a row's sum of squares must stay below 2^128, and mean(x^2) + eps at or
+ *   above 2^-126 (so not 0).  The rest as for lvx_rope_axes.
  * lvx_head_norm_rope_bwd: from the forward's inputs q, k and the gradients
  *   dq_out, dk_out of its outputs, with g = R^T dy, h = 1/sqrt(mean(x^2) + eps),
  *     dx = h (w o g - x h mean(w o g o x h)),   dw = sum over tokens and heads of g o x h.
@@ -374,8 +375,10 @@ lvx_status lvx_head_norm_rope_bwd(const void* q, const void* k, const void* w_q,
 /*
  * Attention of a batch of requests that share one long prefix (the visual keys
  * of a video, say), each with a private suffix cache: the decoding step of many
- * questions about one input.  The prefix's keys are read once for the whole
- * batch.  It is the exact attention of the calls above over another set of
+ * questions about one input.  The prefix's keys are read once for the rows of a
+ * tile, whichever requests they are of: 128, or 16 in small batches, or up to 32 in
+ * fp32 (further tiles find them in L2); short requests read all their keys by
+ * themselves.  It is the exact attention of the calls above over another set of
  * keys: its parts, the prefix's and the suffixes', are block partials (O_i, L_i)
  * combined by the same rescaling (LV-XAttn review page, "What carries the
  * argument").
@@ -393,7 +396,12 @@ lvx_status lvx_head_norm_rope_bwd(const void* q, const void* k, const void* w_q,
  *   S_P == 0 or S_cap == 0 leaves that part out (its pointers are ignored).
  *   scale <= 0 selects 1/sqrt(d).
  *   workspace: lvx_attn_prefix_workspace(...) bytes, 16-byte aligned; not
- *   shared by calls that may run at the same time.
+ *   shared by calls that may run at the same time.  It holds the parts' outputs in
+ *   fp32: every row once for each part of the prefix and each part of a suffix by its
+ *   capacity, as many as fill the machine.
+ *   Arithmetic: scores, statistics and sums are fp32.  In bf16 on the tensor cores the
+ *   weights of the product with V are rounded to bf16 (half a step, 2^-8 relative), as
+ *   in lvx_attn_fwd; fp32 tensors keep them in fp32.
  * The lengths stay on the device: a captured call is replayed with other ones.
  * Constraints (else LVX_ERR_INVALID_ARG): B, H, H_kv, S_Q >= 1, S_P + S_cap >= 1,
  *   H % H_kv == 0, tensors 16-byte aligned.  LVX_ERR_UNSUPPORTED: d > 128 or
