@@ -157,3 +157,16 @@ def test_first_keys_of_minus_infinity_for_some_rows(shape, prefix, suffix):
     kp[..., 0] = ks[..., 0] = 0
     kp[:100, :, 0] = -3e38
     check(*lvx.attention_prefix(*args), args, what=str(plan), kmax=longest)
+
+
+@pytest.mark.parametrize("d", range(8, 129, 8))
+def test_every_head_width(d):
+    """Many parts of few rows in both types, and whole row tiles on the tensor cores."""
+    few, tiles = (2, 4, 2, 1, 9000, 300, d), (24, 12, 4, 100, 300, 1100, d)
+    for shape, dt, kernel in ((few, torch.bfloat16, "rows"), (few, torch.float32, "fp32"), (tiles, torch.bfloat16, "tc")):
+        plan = _plan(*shape, dt=dt)
+        assert plan["prefix"] == plan["suffix"] == kernel and not plan["whole"], plan
+        args = _make(*shape, dt=dt, lens=[shape[5], 0, 77, 256, 299])
+        _garbage(args)
+        check(*lvx.attention_prefix(*args), args, what=f"{plan} {dt}")
+    lvx.lvx_last_device_error()
