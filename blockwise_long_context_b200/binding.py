@@ -10,6 +10,7 @@ extension ``_calls.so``, which takes their arguments in less time.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -191,7 +192,7 @@ def lvx_attn_bwd_accumulate(q, k, v, out, lse, dout, dq, dk, dv, causal: bool = 
         if t.dtype != torch.float32:
             raise TypeError("lvx_attn_bwd_accumulate adds into float32 gradients")
     if workspace is None:
-        workspace = bwd_workspace(q, k, causal)
+        workspace = bwd_workspace(q, k, causal, stream)
     ws = workspace.numel() * workspace.element_size()
     _check(lib().lvx_attn_bwd_accumulate(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
                                          _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), B, H, H_kv, S_Q,
@@ -279,14 +280,19 @@ def _launch(name: str, dev: int, stream, *args) -> None:
         raise LvxError(status, name)
 
 
-def _scratch(nbytes: int, dev: int, stream) -> torch.Tensor:
-    """A workspace for launches on `stream` (None: the current one), from the memory of that stream: what is
-    given the same memory once the workspace is dropped comes after the launches."""
+def _on(stream, dev):
+    """Makes `stream` (a Stream or a raw handle; None: the current one as it is) the current stream."""
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return contextlib.nullcontext()
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(stream, device=dev)
-    with torch.cuda.stream(stream):
+    return torch.cuda.stream(stream)
+
+
+def _scratch(nbytes: int, dev, stream) -> torch.Tensor:
+    """A workspace for launches on `stream` (None: the current one), from the memory of that stream: what is
+    given the same memory once the workspace is dropped comes after the launches."""
+    with _on(stream, dev):
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
@@ -511,11 +517,11 @@ def fwd_workspace(q, k, n_blocks: int, causal: bool = False) -> Optional[torch.T
     return torch.empty(nbytes, dtype=torch.uint8, device=q.device)
 
 
-def bwd_workspace(q, k, causal: bool = False) -> torch.Tensor:
+def bwd_workspace(q, k, causal: bool = False, stream=None) -> torch.Tensor:
     B, S_Q, H, d = q.shape
     S_KV, H_kv = k.shape[1], k.shape[2]
     nbytes = lvx_attn_bwd_workspace(B, H, H_kv, S_Q, S_KV, d, causal, _dt(q))
-    return torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    return _scratch(nbytes, q.device, stream)
 
 
 def fwd_partials_view(workspace: torch.Tensor, n, B, H, S_Q, d):

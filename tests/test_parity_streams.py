@@ -70,3 +70,57 @@ def test_two_explicit_streams_with_other_allocations_in_between(make, raw):
         torch.cuda.synchronize()
         for (out, _call), ref in zip(calls, want):
             assert all(torch.equal(x, y) for x, y in zip(out, ref))
+
+
+def _accumulate(dt):
+    g = torch.Generator().manual_seed(3)
+    t = lambda *s: torch.randn(*s, generator=g).to(dt).cuda()  # noqa: E731
+    q, k, v, do = t(1, 300, 4, 64), t(1, 500, 2, 64), t(1, 500, 2, 64), t(1, 300, 4, 64)
+    out, lse = lvx.attention_forward(q, k, v, 2)
+    grads = [torch.zeros(x.shape, device="cuda") for x in (q, k, v)]
+    return grads, lambda s: lvx.lvx_attn_bwd_accumulate(q, k, v, out, lse, do, *grads, stream=s)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_the_backward_s_workspace_belongs_to_the_launch_stream(dt, raw, monkeypatch):
+    """Nothing is launched, as above."""
+    _, call = _accumulate(dt)
+    torch.cuda.synchronize()
+    used = []
+
+    class Recorder:
+        def lvx_attn_bwd_workspace(self, *a):
+            return real.lvx_attn_bwd_workspace(*a)
+
+        def lvx_attn_bwd_accumulate(self, *a):
+            used.append((a[-3], a[-2]))
+            return 0
+
+    real = lvx.lib()
+    monkeypatch.setattr(lvx, "lib", Recorder)
+    call(_handle(torch.cuda.Stream(), raw))
+    (at, size), = used
+    later = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert all(x.data_ptr() + size <= at or at + size <= x.data_ptr() for x in later)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_accumulating_on_an_explicit_stream_with_other_allocations(dt, raw):
+    grads, call = _accumulate(dt)
+    call(None)
+    want = [x.clone() for x in grads]
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        for x in grads:
+            x.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(5_000_000)
+        call(_handle(side, raw))
+        for n in (1 << 16, 1 << 20, 1 << 22):
+            torch.full((n,), float("nan"), device="cuda")
+        torch.cuda.synchronize()
+        for x, y in zip(grads, want):   # (the order of the atomic additions may differ)
+            assert float((x - y).norm()) <= 1e-4 * float(y.norm())
