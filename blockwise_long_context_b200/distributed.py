@@ -96,13 +96,14 @@ def xattn_forward_sharded(q: torch.Tensor, k_shard: torch.Tensor, v_shard: torch
     if not q.is_cuda:
         raise RuntimeError("xattn_forward_sharded runs in the CUDA library; q must be on a GPU")
     B, S_Q, H, d = q.shape
-    o_loc = torch.empty(n_local_blocks, B, H, S_Q, d, dtype=torch.float32, device=q.device)
-    l_loc = torch.empty(n_local_blocks, B, H, S_Q, dtype=torch.float32, device=q.device)
-    lvx.lvx_attn_fwd_partials(q, k_shard, v_shard, o_loc, l_loc, scale, stream)
-    o_all, l_all = gather_partials(o_loc, l_loc, group)
-    out = torch.empty_like(q)
-    lse = torch.empty(B, H, S_Q, dtype=torch.float32, device=q.device)
-    lvx.lvx_merge_partials(o_all, l_all, out, lse, stream)
+    with lvx._on(stream, q.device):   # the exchanges and the memory go with the kernels
+        o_loc = torch.empty(n_local_blocks, B, H, S_Q, d, dtype=torch.float32, device=q.device)
+        l_loc = torch.empty(n_local_blocks, B, H, S_Q, dtype=torch.float32, device=q.device)
+        lvx.lvx_attn_fwd_partials(q, k_shard, v_shard, o_loc, l_loc, scale)
+        o_all, l_all = gather_partials(o_loc, l_loc, group)
+        out = torch.empty_like(q)
+        lse = torch.empty(B, H, S_Q, dtype=torch.float32, device=q.device)
+        lvx.lvx_merge_partials(o_all, l_all, out, lse)
     return out, lse
 
 
@@ -156,8 +157,9 @@ def xattn_forward_ring(q, k_shard, v_shard, group=None, scale: float = 0.0, stre
     if not q.is_cuda:
         raise RuntimeError("xattn_forward_ring runs in the CUDA library; q must be on a GPU")
     from .ring import RingExchange, kernel_merge, kernel_partial
-    return run_xattn_ring(q, k_shard, v_shard, kernel_partial(scale, stream),
-                          kernel_merge(q, stream), RingExchange(group), n_local_blocks)
+    with lvx._on(stream, q.device):
+        return run_xattn_ring(q, k_shard, v_shard, kernel_partial(scale), kernel_merge(q),
+                              RingExchange(group), n_local_blocks)
 
 
 def _recv_like(t: torch.Tensor, n: int, seq_dim: int = 1) -> torch.Tensor:
@@ -210,9 +212,10 @@ def xattn_backward_ring(q, k_shard, v_shard, out, lse, do, group=None, scale: fl
     if not q.is_cuda:
         raise RuntimeError("xattn_backward_ring runs in the CUDA library; q must be on a GPU")
     from .ring import RingExchange, kernel_block_grad
-    dq, dk, dv = run_xattn_ring_backward(q, k_shard, v_shard, out, lse, do,
-                                         kernel_block_grad(scale, stream), RingExchange(group))
-    return dq.to(q.dtype), dk.to(k_shard.dtype), dv.to(v_shard.dtype)
+    with lvx._on(stream, q.device):
+        dq, dk, dv = run_xattn_ring_backward(q, k_shard, v_shard, out, lse, do,
+                                             kernel_block_grad(scale), RingExchange(group))
+        return dq.to(q.dtype), dk.to(k_shard.dtype), dv.to(v_shard.dtype)
 
 
 def run_xattn_sharded_backward(q, k, v, out, lse, do, grad_fn, group=None):
@@ -236,6 +239,7 @@ def xattn_backward_sharded(q, k_shard, v_shard, out, lse, do, group=None, scale:
     if not q.is_cuda:
         raise RuntimeError("xattn_backward_sharded runs in the CUDA library; q must be on a GPU")
     from .ring import kernel_block_grad
-    dq, dk, dv = run_xattn_sharded_backward(q, k_shard, v_shard, out, lse, do,
-                                            kernel_block_grad(scale, stream), group)
-    return dq.to(q.dtype), dk.to(k_shard.dtype), dv.to(v_shard.dtype)
+    with lvx._on(stream, q.device):
+        dq, dk, dv = run_xattn_sharded_backward(q, k_shard, v_shard, out, lse, do,
+                                                kernel_block_grad(scale), group)
+        return dq.to(q.dtype), dk.to(k_shard.dtype), dv.to(v_shard.dtype)

@@ -278,13 +278,14 @@ def kernel_partial(scale: float = 0.0, stream=None) -> PartialFn:
             o, l = o[:k_blk.shape[1]], l[:k_blk.shape[1]]
         # one step's slice of the partials is 16-byte aligned only if its size is;
         # the library wants aligned pointers, so short shards go through a copy
-        oo = o if o.data_ptr() % 16 == 0 else torch.empty_like(o)
-        ll = l if l.data_ptr() % 16 == 0 else torch.empty_like(l)
-        lvx.lvx_attn_fwd_partials(q, k_blk, v_blk, oo, ll, scale, stream, causal=diagonal)
-        if oo is not o:
-            o.copy_(oo)
-        if ll is not l:
-            l.copy_(ll)
+        with lvx._on(stream, q.device):
+            oo = o if o.data_ptr() % 16 == 0 else torch.empty_like(o)
+            ll = l if l.data_ptr() % 16 == 0 else torch.empty_like(l)
+            lvx.lvx_attn_fwd_partials(q, k_blk, v_blk, oo, ll, scale, causal=diagonal)
+            if oo is not o:
+                o.copy_(oo)
+            if ll is not l:
+                l.copy_(ll)
     return fn
 
 
@@ -292,10 +293,11 @@ def kernel_merge(like: torch.Tensor, stream=None) -> MergeFn:
     """The library's merge kernel, output in ``like``'s dtype (shape from the partials)."""
     def fn(o_parts, l_parts):
         _, B, H, S_r, d = o_parts.shape
-        out = torch.empty((B, S_r, H, d), dtype=like.dtype, device=like.device)
-        lse = torch.empty(B, H, S_r, dtype=torch.float32, device=like.device)
-        if S_r > 0:
-            lvx.lvx_merge_partials(o_parts, l_parts, out, lse, stream)
+        with lvx._on(stream, like.device):
+            out = torch.empty((B, S_r, H, d), dtype=like.dtype, device=like.device)
+            lse = torch.empty(B, H, S_r, dtype=torch.float32, device=like.device)
+            if S_r > 0:
+                lvx.lvx_merge_partials(o_parts, l_parts, out, lse)
         return out, lse
     return fn
 
@@ -324,8 +326,9 @@ def ring_attention_forward(q, k, v, group=None, causal: bool = False, scale: flo
     across the ranks of ``group`` (rows cut with ``rank_bounds``) ->
     out [B, S_r, H, d], lse [B, H, S_r] float32."""
     _require_cuda(q, "ring_attention_forward")
-    return run_ring_forward(q, k, v, kernel_partial(scale, stream), kernel_merge(q, stream),
-                            RingExchange(group), causal, layout)
+    with lvx._on(stream, q.device):   # the exchanges and the memory go with the kernels
+        return run_ring_forward(q, k, v, kernel_partial(scale), kernel_merge(q),
+                                RingExchange(group), causal, layout)
 
 
 def ring_attention_backward(q, k, v, out, lse, do, group=None, causal: bool = False,

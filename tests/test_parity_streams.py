@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from blockwise_long_context_b200 import binding as lvx
+from blockwise_long_context_b200 import distributed, ring
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +125,47 @@ def test_accumulating_on_an_explicit_stream_with_other_allocations(dt, raw):
         torch.cuda.synchronize()
         for x, y in zip(grads, want):   # (the order of the atomic additions may differ)
             assert float((x - y).norm()) <= 1e-4 * float(y.norm())
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_the_sharded_calls_run_on_the_explicit_stream(raw):
+    """One rank of each sharded call while the current stream is busy: what the call fills, computes and frees
+    goes with the given stream."""
+    g = torch.Generator().manual_seed(4)
+    t = lambda *s: torch.randn(*s, generator=g).bfloat16().cuda()  # noqa: E731
+    q, k, v, do = t(1, 256, 4, 64), t(1, 512, 2, 64), t(1, 512, 2, 64), t(1, 256, 4, 64)
+    out, lse = lvx.attention_forward(q, k, v, 1)
+    calls = [lambda s: distributed.xattn_forward_sharded(q, k, v, n_local_blocks=2, stream=s),
+             lambda s: distributed.xattn_forward_ring(q, k, v, n_local_blocks=2, stream=s),
+             lambda s: ring.ring_attention_forward(q, k, v, stream=s),
+             lambda s: distributed.xattn_backward_sharded(q, k, v, out, lse, do, stream=s),
+             lambda s: distributed.xattn_backward_ring(q, k, v, out, lse, do, stream=s)]
+    for call in calls:
+        want = call(None)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        torch.cuda._sleep(50_000_000)   # the current stream's work ends after the call's
+        got = call(_handle(side, raw))
+        side.synchronize()
+        torch.full((1 << 22,), float("nan"), device="cuda")
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):   # (bf16 gradients of sums whose order may differ)
+            assert float((x.float() - y.float()).norm()) <= 1e-2 * float(y.float().norm())
+
+
+def test_a_partial_in_an_unaligned_place_on_an_explicit_stream():
+    """The copy of a partial whose place is not 16-byte aligned goes with the kernel that writes it."""
+    g = torch.Generator().manual_seed(5)
+    q, k, v = (torch.randn(1, s, 1, 64, generator=g).bfloat16().cuda() for s in (3, 512, 512))
+    l_all = torch.zeros(2, 1, 1, 3, device="cuda")   # the second slice: 12 bytes from the first
+    want_o, want_l = torch.zeros(1, 1, 1, 3, 64, device="cuda"), torch.zeros(1, 1, 1, 3, device="cuda")
+    ring.kernel_partial()(q, k, v, want_o, want_l, False)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    o = torch.zeros_like(want_o)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    ring.kernel_partial(stream=side)(q, k, v, o, l_all[1:], False)
+    side.synchronize()
+    assert torch.equal(o, want_o) and torch.equal(l_all[1:], want_l) and (l_all[0] == 0).all()
