@@ -392,7 +392,9 @@ lvx_status lvx_head_norm_rope_bwd(const void* q, const void* k, const void* w_q,
  *   S_Q + t.  With S_Q > 1, values of a request's valid keys must be finite.
  *   lse [B, H, S_Q] float32, natural log.  A row that sees no key gets out = 0,
  *   lse = -inf.  out and lse are what lvx_attn_bwd_accumulate takes to add the
- *   gradients over the prefix and over each suffix.
+ *   gradients: over the prefix for all rows as one batch entry, and for each request
+ *   (n = n_b on the host) over the n - S_Q keys before the tokens, without a mask, and
+ *   the last S_Q keys, causal; where n < S_Q, over the n keys for the last n tokens.
  *   S_P == 0 or S_cap == 0 leaves that part out (its pointers are ignored).
  *   scale <= 0 selects 1/sqrt(d).
  *   workspace: lvx_attn_prefix_workspace(...) bytes, 16-byte aligned; not
