@@ -272,7 +272,7 @@ Cut cut_prefix(PrefixKernel k, const Shape& f, const PrefixProblem& p, long long
 // where parts of 512 make more than four waves of blocks, longer ones until they do not: so many
 // even out nothing, the blocks past the lengths cost their start, and each part takes its rows'
 // output in fp32, in the workspace and in the merge (1024 tokens over 16384 + 16384 keys 500 us,
-// with parts of 512 keys 750; 64 requests of up to 1310 keys in caches of 65536 46 us, 231).
+// with parts of 512 keys 750; 64 requests of up to 1309 keys in caches of 65536 46 us, 231).
 Cut cut_suffix(PrefixKernel k, const Shape& f, const PrefixProblem& p, long long tiles) {
   Cut best = {0, 64, 0.0, 0.0};
   double least = 0.0;
