@@ -26,7 +26,10 @@
 // The running maximum moves only when it grows by more than 2^8, as in the block
 // forward.  P is rounded to bf16 for the product (half a step, at most 2^-8 of each
 // weight), the type in which V and the matrix unit take it; the row sum adds the
-// unrounded fp32 weights.
+// unrounded fp32 weights.  Outputs of independent values are then off by 2.3e-3 (root mean
+// square) where their own rounding alone is 1.65e-3; a second product with what is left of
+// the weights brings them there and takes 115 -> 135 us for 128 requests over 32768 + 1024
+// keys, 250 -> 327 for 8 x 64 tokens over 32768.
 //
 // Keys past a request's length.  The cache behind them may hold anything: their
 // scores are replaced by -inf, and their rows of V are zeroed in shared memory
